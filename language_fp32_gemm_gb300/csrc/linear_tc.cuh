@@ -461,13 +461,15 @@ __global__ void __launch_bounds__(Shape<BN, PASSES, PAIR>::kThreads, 1)
       };
       const bool use_tma = WAY == kAsLaunched ? p.tma != 0 : WAY == kByTma;
       const bool residual_tma = use_tma && p.e.residual;
-      auto first_residuals = [&]() {
-        if (lane == 0 && residual_tma) {
+      // A tile takes the slots in turn from the first: none of the tile's before may still
+      // be read then, whatever its number of blocks was.
+      auto begin_blocks = [&]() {
+        if (lane == 0 && use_tma) {
           block_stores_read(0);
-          for (int b = 0; b < blocks && b < out_slots; ++b) load_residual(b);
+          for (int b = 0; residual_tma && b < blocks && b < out_slots; ++b) load_residual(b);
         }
       };
-      if (it.piece < 0) first_residuals();
+      if (it.piece < 0) begin_blocks();
       float sum[kCols];  // the first partial sum is taken as it is
       const int n_partials = (it.k_hi - it.k_lo + p.promote_blocks - 1) / p.promote_blocks;
       for (int c = 0; c < n_partials; ++c, ++partial) {
@@ -529,7 +531,7 @@ __global__ void __launch_bounds__(Shape<BN, PASSES, PAIR>::kThreads, 1)
           if (arrived == static_cast<unsigned>(p.pieces)) *counter = 0u;  // for the next launch
         }
         if (__shfl_sync(0xffffffffu, arrived, 0) != static_cast<unsigned>(p.pieces)) continue;
-        first_residuals();
+        begin_blocks();
         constexpr int kBatch = kF4 < 8 ? kF4 : 8;
 #pragma unroll
         for (int v0 = 0; v0 < kF4; v0 += kBatch) {

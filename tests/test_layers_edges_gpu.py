@@ -1,0 +1,47 @@
+"""The layer operators where their kernels take turns, run long or meet extreme values."""
+import pytest
+
+import layers_ref as ref
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from language_fp32_gemm_gb300 import layers  # noqa: E402
+from test_layers_gpu import BF16, E4M3, F16, F32, IDS, TYPES, dev, normal, vector, weight  # noqa: E402, F401
+
+
+def small_integers(rows, cols, dtype, seed):
+    """-1, 0 or 1: sums of up to 256 products are exact in every type."""
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    return torch.randint(-1, 2, (rows, cols), generator=g, device="cuda").to(dtype)
+
+
+# More tiles than SMs, short contractions, and columns that leave a tile with fewer output blocks
+# than a warp has places for: one tile's stores are still on their way when the next one's begin.
+# Exact sums, so that a block stored twice, late or over another shows in any element.
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("preact", [False, True], ids=["out", "out+z"])
+@pytest.mark.parametrize("M,N,K", [(40000, 64, 64), (40000, 32, 64), (8192, 192, 64), (64, 60000, 64), (32, 60000, 64),
+                                   (16, 60000, 128), (40, 60008, 64), (8192, 4104, 64), (8192, 4128, 128)])
+def test_many_tiles_without_a_residual(M, N, K, preact, dtype):
+    x, w = small_integers(M, K, dtype, 1), small_integers(N, K, dtype, 2).t()
+    want = x.float() @ w.float()
+    assert torch.equal(want, want.round()) and want.abs().max() <= K
+    for _ in range(5):
+        out, z = torch.full_like(want, 7.0, dtype=dtype), torch.full_like(want, 7.0, dtype=dtype)
+        if preact:
+            layers.linear(x, w, act="relu", out=out, preact=z, save_preact=True, products="tensor")
+            assert torch.equal(z.float(), want) and torch.equal(out.float(), want.clamp(min=0))
+        else:
+            layers.linear(x, w, out=out, products="tensor")
+            assert torch.equal(out.float(), want)
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+def test_many_tiles_of_gradients(dtype):
+    M, N, K = 8192, 64, 4128
+    x, w, dout = small_integers(M, K, dtype, 1), small_integers(K, N, dtype, 2), small_integers(M, N, dtype, 3)
+    dx_want, dw_want = dout.float() @ w.float().t(), x.float().t() @ dout.float()
+    for _ in range(5):
+        dx, dw, _ = layers.linear_backward(dout, x, w, need_dbias=False, grad_dtype=F32, products="tensor")
+        assert torch.equal(dx.float(), dx_want) and torch.equal(dw, dw_want)
