@@ -88,7 +88,7 @@ __device__ __forceinline__ void store4(int type, void *base, int64_t i, int n, b
 
 // V consecutive elements as they are stored.  load and store: the first n exist (zeros
 // elsewhere), and with V > 1 the address is aligned for all of them at once;
-// store_any: any alignment.  16-bit types are converted in pairs.
+// load_any and store_any: any alignment.  16-bit types are converted in pairs.
 template <int TYPE, int V>
 struct Group {
   using T = typename Elem<TYPE>::T;
@@ -103,6 +103,11 @@ struct Group {
 #pragma unroll
       for (int j = 0; j < V; ++j) x[j] = j < n ? p[j] : Elem<TYPE>::store(0.f);
     }
+  }
+  __device__ __forceinline__ void load_any(const void *base, int64_t i, int n) {
+    const T *p = static_cast<const T *>(base) + i;
+#pragma unroll
+    for (int j = 0; j < V; ++j) x[j] = j < n ? p[j] : Elem<TYPE>::store(0.f);
   }
   __device__ __forceinline__ void store_any(void *base, int64_t i, int n) const {
     T *p = static_cast<T *>(base) + i;

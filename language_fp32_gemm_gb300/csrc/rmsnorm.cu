@@ -198,9 +198,11 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
   }
   for (int col = ITEMS * step + t * V; col < a.cols; col += step) {
     G hg, wg;
-    // what this thread stored, where it can be loaded as a group
-    if (a.sum && (V == 1 || a.vec_out)) hg.load(a.sum, row * a.sum_ld + col, a.cols - col);
-    else load_h(col, a.cols - col, hg);
+    // What this thread stored: the sum may lie over x or the residual, which then are gone.
+    const int64_t at = row * a.sum_ld + col;
+    if (!a.sum) hg.load(a.x, row * a.x_ld + col, a.cols - col);
+    else if (a.vec_out) hg.load(a.sum, at, a.cols - col);
+    else hg.load_any(a.sum, at, a.cols - col);
     load_weight(a.weight, col, a.cols - col, wg);
     put_normed(a, row, col, hg, wg, factor);
   }

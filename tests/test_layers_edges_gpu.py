@@ -45,3 +45,41 @@ def test_many_tiles_of_gradients(dtype):
     for _ in range(5):
         dx, dw, _ = layers.linear_backward(dout, x, w, need_dbias=False, grad_dtype=F32, products="tensor")
         assert torch.equal(dx.float(), dx_want) and torch.equal(dw, dw_want)
+
+
+LONG = [(3, 4097), (5, 1000), (400, 1003), (2, 16384), (2, 20001), (2, 33001), (1, 40001)]
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("over", ["residual", "x"])
+@pytest.mark.parametrize("pad_out", [0, 8])
+@pytest.mark.parametrize("size", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_rmsnorm_sum_over_an_input(size, pad_out, over, dtype):
+    # inputs on 16-byte boundaries, outputs there or not; rows within the registers and beyond them
+    rows, cols = size
+    x, r = (normal(size, dtype, i, 1.0, pad=-cols % 8) for i in (1, 2))
+    w = (1 + 0.1 * vector(cols, F32, 3)).to(dtype)
+    h = (x.float() + r.float()).to(dtype)
+    want, bound = ref.rmsnorm(h, w, 1e-6)
+    y0 = torch.empty(rows, cols + (-cols % 8 if pad_out else 0), dtype=dtype, device="cuda")[:, :cols]
+    q0 = torch.empty(rows, cols + (-cols % 16 if pad_out else 0), dtype=E4M3, device="cuda")[:, :cols]
+    for eight_bit in (False, True):
+        a, b = (torch.empty_strided(t.shape, t.stride(), dtype=dtype, device="cuda").copy_(t) for t in (x, r))
+        if eight_bit:
+            q, scale, got = layers.rmsnorm_q8(a, w, b, out=q0, sum=b if over == "residual" else a)
+            s = ref.f64(scale)[:, None]
+            ref.check(ref.f64(q) * s, want, bound + s * (2.0 ** -4 * (want / s).abs() + 2.0 ** -10) * (1 + 2.0 ** -20), "q")
+        else:
+            y, got = layers.rmsnorm(a, w, b, out=y0, sum=b if over == "residual" else a)
+            ref.check(y, want, ref.rounded(bound, want, dtype), "y")
+        assert torch.equal(got, h) and got.data_ptr() == (b if over == "residual" else a).data_ptr()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("size", LONG, ids=lambda s: "x".join(map(str, s)))
+def test_rmsnorm_gradient_over_dsum(size, dtype):
+    rows, cols = size
+    h, dy, ds = (normal(size, dtype, i, 1.0, pad=-cols % 8) for i in (1, 2, 3))
+    dx, dw = layers.rmsnorm_backward(dy, h, None, ds)
+    over, dw2 = layers.rmsnorm_backward(dy, h, None, ds, dx=ds)
+    assert over.data_ptr() == ds.data_ptr() and torch.equal(over, dx) and torch.equal(dw, dw2)
