@@ -512,8 +512,9 @@ __global__ void __launch_bounds__(Shape<BN, PASSES, PAIR>::kThreads, 1)
         // Leave the piece's sum in its slot (float4 v of lane l at v * 32 + l) and
         // count in; the last piece of the tile adds all of them in order (its own too:
         // kept in registers beside the others' they spilled, 10 % at 8192^3).  One
-        // atomic a warp releases the lanes' stores (which the barrier orders before it)
-        // and acquires the other pieces'.
+        // atomic a warp releases the lanes' stores and acquires the other pieces': the
+        // barriers order the lanes' stores before it and their loads after it (a shuffle
+        // orders no memory).
         constexpr int kF4 = kCols / 4;
         constexpr int64_t kSlot = static_cast<int64_t>(PAIR ? 2 : 1) * S::kEpiWarps * kF4 * 32;
         const int jt = it.tile - p.full_tiles;
@@ -531,6 +532,7 @@ __global__ void __launch_bounds__(Shape<BN, PASSES, PAIR>::kThreads, 1)
           if (arrived == static_cast<unsigned>(p.pieces)) *counter = 0u;  // for the next launch
         }
         if (__shfl_sync(0xffffffffu, arrived, 0) != static_cast<unsigned>(p.pieces)) continue;
+        __syncwarp();
         begin_blocks();
         constexpr int kBatch = kF4 < 8 ? kF4 : 8;
 #pragma unroll

@@ -83,3 +83,16 @@ def test_rmsnorm_gradient_over_dsum(size, dtype):
     dx, dw = layers.rmsnorm_backward(dy, h, None, ds)
     over, dw2 = layers.rmsnorm_backward(dy, h, None, ds, dx=ds)
     assert over.data_ptr() == ds.data_ptr() and torch.equal(over, dx) and torch.equal(dw, dw2)
+
+
+# Tiles cut along the contraction: pieces' sums meet in the workspace.  Exact sums.
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("residual", [False, True], ids=["", "residual"])
+@pytest.mark.parametrize("M,N,K", [(16, 8192, 8192), (5, 300, 16384), (600, 520, 4096), (300, 264, 2080), (3000, 136, 4096)])
+def test_pieces_of_tiles(M, N, K, residual, dtype):
+    x, w = small_integers(M, K, dtype, 1), small_integers(N, K, dtype, 2).t()
+    r = small_integers(M, N, F32, 3) if residual else None
+    want = x.float() @ w.float() + (r if residual else 0.0)
+    for _ in range(5):
+        out = layers.linear(x, w, residual=r, out_dtype=F32, products="tensor")
+        assert torch.equal(out, want)
