@@ -145,6 +145,12 @@ __device__ __forceinline__ void load_weight(const void *weight, int col, int n, 
   else w.fill(1.f);
 }
 
+// A thread's next column of a row; a step of up to 8192 from within the longest rows
+// (2^31 - 1024) passes 2^31, and stops short of it instead.
+__device__ __forceinline__ int next_col(int col, int step) {
+  return static_cast<int>(min(static_cast<unsigned>(col) + static_cast<unsigned>(step), 0x7fffffffu));
+}
+
 template <int TYPE, int V, int ITEMS, int THREADS>
 __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     rmsnorm_kernel(const __grid_constant__ NormArgs a) {
@@ -182,7 +188,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     if (a.sum) put_group(h[i], a.sum, row * a.sum_ld + col, a.cols - col, a.vec_out);
     add_statistics(h[i], w[i], ss, top);
   }
-  for (int col = ITEMS * step + t * V; col < a.cols; col += step) {  // the rest of a longer row
+  for (int col = ITEMS * step + t * V; col < a.cols; col = next_col(col, step)) {  // the rest of a longer row
     G hg, wg;
     load_h(col, a.cols - col, hg);
     load_weight(a.weight, col, a.cols - col, wg);
@@ -196,7 +202,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     const int col = i * step + t * V;
     put_normed(a, row, col, h[i], w[i], factor);
   }
-  for (int col = ITEMS * step + t * V; col < a.cols; col += step) {
+  for (int col = ITEMS * step + t * V; col < a.cols; col = next_col(col, step)) {
     G hg, wg;
     // What this thread stored: the sum may lie over x or the residual, which then are gone.
     const int64_t at = row * a.sum_ld + col;
@@ -381,7 +387,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS <= 128 
     };
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) sums(i * step + t * V, h[i], dy[i]);
-    for (int col = ITEMS * step + t * V; col < a.cols; col += step) {
+    for (int col = ITEMS * step + t * V; col < a.cols; col = next_col(col, step)) {
       G hg, dg;
       hg.load(a.h, row * a.h_ld + col, a.cols - col);
       dg.load(a.dy, row * a.dy_ld + col, a.cols - col);
@@ -398,7 +404,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS, THREADS <= 128 
     };
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) put(i * step + t * V, h[i], dy[i], ds[i], dw[i]);
-    for (int col = ITEMS * step + t * V; col < a.cols; col += step) {
+    for (int col = ITEMS * step + t * V; col < a.cols; col = next_col(col, step)) {
       G hg, dg, sg;
       float sum[V] = {};
       hg.load(a.h, row * a.h_ld + col, a.cols - col);

@@ -7,6 +7,7 @@ pytestmark = pytest.mark.gpu
 torch = pytest.importorskip("torch")
 
 from language_fp32_gemm_gb300 import layers  # noqa: E402
+import language_fp32_gemm_gb300 as phobos  # noqa: E402
 from test_layers_gpu import BF16, E4M3, F16, F32, IDS, TYPES, dev, normal, vector, weight  # noqa: E402, F401
 
 
@@ -96,3 +97,22 @@ def test_pieces_of_tiles(M, N, K, residual, dtype):
     for _ in range(5):
         out = layers.linear(x, w, residual=r, out_dtype=F32, products="tensor")
         assert torch.equal(out, want)
+
+
+def test_rmsnorm_of_the_longest_row():
+    # 2^31 - 1024 columns: a thread's last step passes 2^31.  Ones times two: every sum is exact
+    # (2^21 or fewer squares of four a thread), rstd and y are known to the bit in bf16.
+    cols = (1 << 31) - 1024
+    x = torch.full((1, cols), 2.0, dtype=BF16, device="cuda")
+    y = layers.rmsnorm(x)
+    assert y.shape == x.shape and (y == 1.0).all()
+    del y
+    q, scale = layers.rmsnorm_q8(x)
+    assert (q.view(torch.uint8) == 0x7E).all() and abs(scale.item() * 448 - 1) < 2.0 ** -20
+    del q
+    # dy = h: dx = rstd (dy - n mean(dy n)) is h's rounding errors times rstd, dweight = 2 n
+    dx, dw = layers.rmsnorm_backward(x, x)
+    assert dx.abs().max() <= 2.0 ** -18 and (dw == 2.0).all()
+    del x, dx, dw
+    phobos.phobos_release()
+    torch.cuda.empty_cache()
