@@ -75,16 +75,24 @@ __device__ __forceinline__ void row_reduce(float &a, float &b, int t, float2 *sc
   b = s.y;
 }
 
-// What h w is multiplied with, from the row's sum of h^2 and largest |h w|; `first`
-// stores the scale.
-__device__ __forceinline__ float row_factor(const NormArgs &a, float ss, float top, int64_t row, bool first) {
-  const float rstd = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
-  if (!a.q8) return rstd;
-  const float amax = top * rstd;
+// y = h rstd w, q = y inv_scale.  Two factors: of a row of small numbers, rstd may be
+// 1 / sqrt(eps) and inv_scale 2^126, whose product is not finite.
+struct RowFactors {
+  float rstd, inv_scale;
+};
+
+// From the row's sum of h^2 and largest |h w|; `first` stores the scale.
+__device__ __forceinline__ RowFactors row_factors(const NormArgs &a, float ss, float top, int64_t row, bool first) {
+  RowFactors f;
+  f.rstd = rsqrtf(ss / static_cast<float>(a.cols) + a.eps);
+  f.inv_scale = 1.f;
+  if (!a.q8) return f;
+  const float amax = top * f.rstd;
   // not below the smallest normal number, whose reciprocal is finite
   const float s = amax == 0.f ? 1.f : fmaxf(amax / 448.f, 1.17549435e-38f);
   if (first) a.scale[row] = isnan(ss) ? ss : s;
-  return rstd / s;
+  f.inv_scale = 1.f / s;
+  return f;
 }
 
 // Outputs whose rows are not aligned are stored element by element.
@@ -96,14 +104,16 @@ __device__ __forceinline__ void put_group(const G &g, void *base, int64_t i, int
 
 template <typename G>
 __device__ __forceinline__ void put_normed(const NormArgs &a, int64_t row, int col, const G &h, const G &w,
-                                           float factor) {
+                                           const RowFactors &f) {
   constexpr int V = G::kSize;
   float v[V], wv[V];
   h.unpack(v);
   w.unpack(wv);
 #pragma unroll
-  for (int j = 0; j < V; ++j) v[j] = v[j] * factor * wv[j];
+  for (int j = 0; j < V; ++j) v[j] = v[j] * f.rstd * wv[j];
   if (a.q8) {
+#pragma unroll
+    for (int j = 0; j < V; ++j) v[j] *= f.inv_scale;
     store_q<V>(a.out, row * a.out_ld + col, a.cols - col, a.vec_out, v);
   } else {
     G y;
@@ -196,11 +206,11 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     add_statistics(hg, wg, ss, top);
   }
   row_reduce<THREADS, true>(ss, top, t, scratch);
-  const float factor = row_factor(a, ss, top, row, t == 0);
+  const RowFactors factors = row_factors(a, ss, top, row, t == 0);
 #pragma unroll
   for (int i = 0; i < ITEMS; ++i) {
     const int col = i * step + t * V;
-    put_normed(a, row, col, h[i], w[i], factor);
+    put_normed(a, row, col, h[i], w[i], factors);
   }
   for (int col = ITEMS * step + t * V; col < a.cols; col = next_col(col, step)) {
     G hg, wg;
@@ -210,7 +220,7 @@ __global__ void __launch_bounds__(THREADS == 32 ? 256 : THREADS)
     else if (a.vec_out) hg.load(a.sum, at, a.cols - col);
     else hg.load_any(a.sum, at, a.cols - col);
     load_weight(a.weight, col, a.cols - col, wg);
-    put_normed(a, row, col, hg, wg, factor);
+    put_normed(a, row, col, hg, wg, factors);
   }
 }
 
@@ -300,11 +310,11 @@ __global__ void __launch_bounds__(THREADS, THREADS >= 512 ? 1 : 512 / THREADS)
       add_statistics(h[i], w[i], ss, top);
     }
     row_reduce<THREADS, true>(ss, top, t, scratch[turn]);
-    const float factor = row_factor(a, ss, top, row, t == 0);
+    const RowFactors factors = row_factors(a, ss, top, row, t == 0);
 #pragma unroll
     for (int i = 0; i < ITEMS; ++i) {
       const int col = (i * THREADS + t) * V;
-      put_normed(a, row, col, h[i], w[i], factor);
+      put_normed(a, row, col, h[i], w[i], factors);
     }
     slot = slot + 1 == Ring::kRows ? 0 : slot + 1;
   }

@@ -116,3 +116,23 @@ def test_rmsnorm_of_the_longest_row():
     del x, dx, dw
     phobos.phobos_release()
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=IDS.get)
+@pytest.mark.parametrize("rows,cols", [(4, 300), (5, 4096), (400, 2048), (3, 1001)])
+def test_rmsnorm_q8_of_small_numbers(rows, cols, dtype):
+    # rows from 1e-34 down to the smallest normal numbers, with zeros among them: eps decides rstd
+    x = normal((rows, cols), F32, 1) * torch.logspace(-34, -38, rows, device="cuda")[:, None]
+    x[:, ::3] = 0
+    x = x.to(dtype)
+    q, scale = layers.rmsnorm_q8(x)
+    want, bound = ref.rmsnorm(x, None, 1e-6)
+    amax = want.abs().amax(1)
+    s = ref.f64(scale)
+    exact = (amax / 448).clamp(min=2.0 ** -126)
+    assert ((s - exact).abs() <= 2.0 ** -20 * exact).all()
+    # below the least scale, q loses what half of e4m3's smallest step leaves: 2^-10 of the scale.
+    # Below 2^-126 fp32 products round by up to 2^-150.
+    s = s[:, None]
+    ref.check(ref.f64(q) * s, want, bound + s * (2.0 ** -4 * (want / s).abs() + 2.0 ** -10) * (1 + 2.0 ** -20) + 2.0 ** -148, "q")
+    assert not q[:, ::3].float().any()
