@@ -283,12 +283,14 @@ phobos_status_t run_tc(const LinearArgs &l, const Runtime &rt, cudaStream_t stre
   t.group = std::min(plan.tiles_r, 16);
   t.k_blocks = k_blocks;
   // Truncating MMA updates per partial sum: 36 of three fp16 products (24 for short
-  // contractions); 32 for fp32 outputs; 512 for 16-bit ones, whose own rounding is
-  // 2^-11 or 2^-8 (each update loses 2^-24 or less of the sum on average; with 128,
-  // bf16 8192^3 takes 2 % more time).  fp32, norm of the error over the norm of the result at any
-  // K, and time at 4096^3: 1 block 2.7e-7, 414 us; 2 blocks 4.8e-7, 351; 3 blocks
-  // 6.9e-7, 334; 4 blocks 9.3e-7, 327.
-  t.promote_blocks = l.type == PHOBOS_TYPE_F32 ? (l.K <= 512 ? 2 : 3) : l.e.type == PHOBOS_TYPE_F32 ? 8 : 128;
+  // contractions); 32 for fp32 outputs; 128 for 16-bit ones, whose own rounding is
+  // 2^-11 or 2^-8.  An update loses up to 2^-23 of the sum so far, so that 128 of them and
+  // up to 32 roundings stay within 2^-15 of the terms' magnitudes; with 512, a sum of one
+  // large and many small terms of its sign did not.  (bf16 8192^3 with everything: 746 us,
+  // with 512 updates 742, with 32 787 to 814; 8 bits 4096 x 8192 x 8192: 196, 196, 212.)
+  // fp32, norm of the error over the norm of the result at any K, and time at 4096^3: 1
+  // block 2.7e-7, 414 us; 2 blocks 4.8e-7, 351; 3 blocks 6.9e-7, 334; 4 blocks 9.3e-7, 327.
+  t.promote_blocks = l.type == PHOBOS_TYPE_F32 ? (l.K <= 512 ? 2 : 3) : l.e.type == PHOBOS_TYPE_F32 ? 8 : 32;
   t.full_tiles = plan.full_tiles;
   t.pieces = plan.pieces;
   t.items = plan.full_tiles + static_cast<int>(tail) * plan.pieces;

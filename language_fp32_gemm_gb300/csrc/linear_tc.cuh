@@ -15,8 +15,8 @@
 // terms each (linear_prep.cu) and three products are summed, small ones first.
 //
 // The tensor cores' fp32 accumulation truncates, so a partial sum spans at most
-// promote_blocks stages (32 or 48 MMA updates) before it is added, with
-// rounding, into registers.
+// promote_blocks stages (24 or 36 MMA updates for fp32 operands, 32 for fp32 outputs
+// of others, 128 for 16-bit outputs) before it is added, with rounding, into registers.
 //
 // Tiles: 256 x 256 on a pair for large outputs; 128 x {16, 32, 64, 128} on one CTA
 // for few columns, with the output transposed (SWAP) when those columns are the

@@ -136,3 +136,46 @@ def test_rmsnorm_q8_of_small_numbers(rows, cols, dtype):
     s = s[:, None]
     ref.check(ref.f64(q) * s, want, bound + s * (2.0 ** -4 * (want / s).abs() + 2.0 ** -10) * (1 + 2.0 ** -20) + 2.0 ** -148, "q")
     assert not q[:, ::3].float().any()
+
+
+# Sums of one sign, where truncation in tensor memory adds up.  The residual takes the sum away
+# again, so that the output's own rounding does not hide the error.  Whole tiles (76 pairs of SMs
+# have one each), so that each sums all of K.
+WHOLE_TILES = 1024, 4864
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16], ids=IDS.get)
+@pytest.mark.parametrize("K", [8192, 16384])
+def test_one_large_term_and_many_small_ones(K, dtype):
+    # each 16 products after the first add 1.75 2^-24 of the sum: less than its last bit
+    M, N = WHOLE_TILES
+    x = torch.full((M, K), 64.0, dtype=dtype, device="cuda")
+    w = torch.zeros(N, K, dtype=dtype, device="cuda")
+    w[:, ::16] = 1.75 * 2.0 ** -20
+    w[:, 0] = 16.0
+    r = torch.full((M, N), -1024.0, dtype=dtype, device="cuda")
+    want, _, bound, _ = ref.linear(x[:1], w.t()[:, :1], None, r[:1, :1])
+    out = layers.linear(x, w.t(), residual=r, products="tensor")
+    ref.check(out, want.expand(M, N), bound.expand(M, N), "out")
+
+
+@pytest.mark.parametrize("dtype", [F16, BF16, E4M3], ids={F16: "f16", BF16: "bf16", E4M3: "e4m3"}.get)
+@pytest.mark.parametrize("K", [8192, 16384])
+def test_sums_of_one_sign(K, dtype):
+    M, N = WHOLE_TILES
+    g = torch.Generator(device="cuda").manual_seed(K)
+    x = torch.rand(M, K, generator=g, device="cuda").to(dtype)
+    w = (torch.rand(N, K, generator=g, device="cuda") * (0.5 if dtype == E4M3 else 2.0 ** -5)).to(dtype)
+    rows = [*range(4), *range(M - 4, M)]
+    out_dtype = BF16 if dtype == E4M3 else dtype
+    scales = (torch.ones(M, device="cuda"), torch.full((N,), 2.0 ** -4, device="cuda")) if dtype == E4M3 else (None, None)
+    part = None if dtype != E4M3 else scales[0][rows]
+    z = ref.linear(x[rows], w.t(), None, None, "none", part, scales[1], out_dtype)[1]
+    r = torch.zeros(M, N, dtype=out_dtype, device="cuda")
+    r[rows] = (-z).to(out_dtype).cuda()
+    want, _, bound, _ = ref.linear(x[rows], w.t(), None, r[rows], "none", part, scales[1], out_dtype)
+    if dtype == E4M3:
+        out = layers.linear_q8(x, scales[0], w.t(), scales[1], residual=r, out_dtype=out_dtype, products="tensor")
+    else:
+        out = layers.linear(x, w.t(), residual=r, products="tensor")
+    ref.check(out[rows], want, bound, "out")
