@@ -207,9 +207,10 @@ __device__ __forceinline__ float activate_slope(float z) {
 
 // --------------------------------------------------------------------- epilogue
 
-// s * 2^e for |e| <= 252 in two factors, so that neither overflows or vanishes
-// when the product does not.
+// s * 2^e in two factors, so that neither overflows or vanishes when the product does
+// not; e <= 254, and below -252 the product is as good as zero (|s| < 2^100).
 __device__ __forceinline__ float times_pow2(float s, int e) {
+  e = max(e, -252);
   const int half = e >> 1;
   return s * __int_as_float((half + 127) << 23) * __int_as_float((e - half + 127) << 23);
 }

@@ -25,22 +25,20 @@ namespace phobos {
 
 namespace {
 
-// The exponent that brings a row with largest magnitude bits `amax` to [2^14, 2^15).
-// Clamped so that both powers of two are normal: rows below 2^-100 keep their
-// absolute accuracy, and a row with an infinity or a NaN is not finite anyway.
+// The exponent that brings a row with largest magnitude bits `amax` to [2^14, 2^15);
+// a row of zeros, or with an infinity or a NaN, takes any.
 __device__ __forceinline__ int row_exponent(unsigned amax) {
-  const int e = static_cast<int>(amax >> 23) - 127;
-  return min(max(e, -100), 127) - 14;
+  const int e = amax >> 23 ? static_cast<int>(amax >> 23) - 127 : 31 - __clz(amax | 1u) - 149;
+  return min(e, 127) - 14;
 }
-__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }
 __device__ __forceinline__ unsigned magnitude(float x) { return __float_as_uint(x) & 0x7FFFFFFFu; }
 
 __device__ __forceinline__ void split_store4(void *hi, void *lo, int64_t i, int n, const float (&v)[4],
-                                             float scale) {
+                                             const int (&e)[4]) {
   float h[4], l[4];
 #pragma unroll
   for (int t = 0; t < 4; ++t) {
-    const float x = v[t] * scale;
+    const float x = times_pow2(v[t], -e[t]);
     h[t] = __half2float(__float2half_rn(x));
     l[t] = x - h[t];
   }
@@ -78,13 +76,13 @@ __device__ __forceinline__ void split_rows(const PrepArgs &a, int block, SplitSh
   }
   const int e = row_exponent(m);
   if (t == 0) a.exp[row] = e;
-  const float scale = pow2(-e);
+  const int e4[4] = {e, e, e, e};
 #pragma unroll 4
   for (int k = t * 4; k < a.k; k += THREADS * 4) {
     float v[4];
     const int n = min(4, a.k - k);
     load4<PHOBOS_TYPE_F32>(a.in.ptr, row * a.in.ld + k, n, a.vec, v);
-    split_store4(a.hi, a.lo, row * a.ld + k, n, v, scale);
+    split_store4(a.hi, a.lo, row * a.ld + k, n, v, e4);
   }
 }
 
@@ -141,10 +139,8 @@ __device__ __forceinline__ void split_strided(const PrepArgs &a, int block, int 
   if (n > 0) {
     if (share == 0 && ty == 0)
       for (int j = 0; j < n; ++j) a.exp[r + j] = e[j];
-    each([&](int k, float (&v)[4]) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] *= pow2(-e[j]);
-      if (k < k1) split_store4(a.hi, a.lo, k * a.ld + r, n, v, 1.0f);
+    each([&](int k, const float (&v)[4]) {
+      if (k < k1) split_store4(a.hi, a.lo, k * a.ld + r, n, v, e);
     });
   }
   if (ctas > 1) cluster_sync();  // the peers read this CTA's maxima until here

@@ -179,3 +179,22 @@ def test_sums_of_one_sign(K, dtype):
     else:
         out = layers.linear(x, w.t(), residual=r, products="tensor")
     ref.check(out[rows], want, bound, "out")
+
+
+@pytest.mark.parametrize("layout", ["nk", "kn"])
+@pytest.mark.parametrize("small", ["x", "w"])
+@pytest.mark.parametrize("M,N,K", [(40, 64, 300), (300, 600, 1024), (900, 1100, 2048)])
+def test_fp32_rows_of_the_smallest_numbers(M, N, K, small, layout):
+    # rows of one operand from 2^-90 to 2^-135, below the normal numbers, against large ones: the
+    # products are ordinary numbers, and each output keeps its own relative accuracy
+    x, w = normal((M, K), F32, 1), normal((K, N), F32, 2)
+    down = torch.linspace(-90, -135, M if small == "x" else N, device="cuda", dtype=torch.float64).round()
+    if small == "x":
+        x, w = (x.double() * torch.exp2(down)[:, None]).float(), w * 2.0 ** 100
+    else:
+        x, w = x * 2.0 ** 100, (w.double() * torch.exp2(down)[None, :]).float()
+    w = w.t().contiguous().t() if layout == "nk" else w
+    want, _, bound, _ = ref.linear(x, w)
+    ref.check(layers.linear(x, w, products="tensor"), want, bound, "out")
+    # both small: nothing is left
+    assert not layers.linear(x[:2] * 2.0 ** -126, w * 2.0 ** -126, products="tensor").any()
