@@ -188,19 +188,23 @@ __device__ __forceinline__ void activate_all(int act, float (&z)[N]) {
   }
 }
 
+// Far from zero the slope is that of z or of zero: the terms that vanish there are left
+// out, as their other factors may have overflowed (infinite z, whose products with zero
+// are NaNs; the cube of a finite one).
 template <int ACT>
 __device__ __forceinline__ float activate_slope(float z) {
   if (ACT == PHOBOS_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
-  if (ACT == PHOBOS_ACT_GELU)  // Phi(z) + z phi(z), phi(0) = 1 / sqrt(2 pi)
-    return fmaf(z * 0.3989422804014327f, __expf(-0.5f * z * z),
-                0.5f * (1.0f + erff(z * 0.70710678118654752f)));
+  if (ACT == PHOBOS_ACT_GELU) {  // Phi(z) + z phi(z), phi(0) = 1 / sqrt(2 pi)
+    const float cdf = 0.5f * (1.0f + erff(z * 0.70710678118654752f)), e = __expf(-0.5f * z * z);
+    return e == 0.0f ? cdf : fmaf(z * 0.3989422804014327f, e, cdf);
+  }
   if (ACT == PHOBOS_ACT_GELU_TANH) {
-    const float p = logistic(kGeluIn * z * fmaf(kGeluCubic * z, z, 1.0f));
-    return fmaf(z * p * (1.0f - p), kGeluIn * fmaf(3.0f * kGeluCubic * z, z, 1.0f), p);
+    const float p = logistic(kGeluIn * z * fmaf(kGeluCubic * z, z, 1.0f)), q = p * (1.0f - p);
+    return q == 0.0f ? p : fmaf(z * q, kGeluIn * fmaf(3.0f * kGeluCubic * z, z, 1.0f), p);
   }
   if (ACT == PHOBOS_ACT_SILU) {
-    const float p = logistic(z);
-    return p * fmaf(z, 1.0f - p, 1.0f);
+    const float p = logistic(z), q = 1.0f - p;
+    return p == 0.0f || q == 0.0f ? p : p * fmaf(z, q, 1.0f);
   }
   return 1.0f;
 }

@@ -198,3 +198,19 @@ def test_fp32_rows_of_the_smallest_numbers(M, N, K, small, layout):
     ref.check(layers.linear(x, w, products="tensor"), want, bound, "out")
     # both small: nothing is left
     assert not layers.linear(x[:2] * 2.0 ** -126, w * 2.0 ** -126, products="tensor").any()
+
+
+@pytest.mark.parametrize("dtype", TYPES, ids=IDS.get)
+@pytest.mark.parametrize("act", ref.ACTS[1:])
+def test_slopes_far_from_zero(act, dtype):
+    # one where z is large, zero where it is large and negative: up to the type's largest value, and
+    # for the infinity that a pre-activation beyond it becomes.  A NaN stays.
+    far = torch.tensor([60.0, 104.0, 1e4, 2e19, 1e30, float("inf")])
+    far = far[(far <= torch.finfo(dtype).max) | far.isinf()]
+    z = torch.cat([far, -far, torch.tensor([float("nan")])]).to(dtype).cuda()[None, :]
+    n = len(far)
+    dout = torch.ones_like(z)
+    x, w = torch.ones(1, 1, dtype=dtype, device="cuda"), torch.ones(1, z.shape[1], dtype=dtype, device="cuda")
+    _, _, db = layers.linear_backward(dout, x, w, z, act, need_dx=False, need_dw=False)
+    assert (db[:n] == 1).all() and (db[n:2 * n].abs() <= 2.0 ** -40).all()
+    assert db[-1].isnan() if act != "relu" else db[-1] == 0
