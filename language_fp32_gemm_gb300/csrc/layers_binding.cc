@@ -8,6 +8,7 @@
 #include <Python.h>
 
 #include <ATen/ATen.h>
+#include <c10/core/GradMode.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -43,10 +44,17 @@ long long ll(int64_t x) { return static_cast<long long>(x); }
 
 // ------------------------------------------------------------------- arguments
 
+// Autograd does not see these calls, so what it would record is refused rather than lost.
 const Tensor *optional_tensor(PyObject *o, const char *name) {
   if (o == Py_None) return nullptr;
   if (!THPVariable_Check(o)) raise(PyExc_TypeError, "%s must be a tensor", name);
-  return &THPVariable_Unpack(o);
+  const Tensor &t = THPVariable_Unpack(o);
+  if (t.requires_grad() && c10::GradMode::is_enabled())
+    raise(PyExc_ValueError,
+          "%s requires grad, which the layer operators do not record: call them under torch.no_grad() (as inside "
+          "a torch.autograd.Function), or detach it",
+          name);
+  return &t;
 }
 
 const Tensor &tensor(PyObject *o, const char *name) {
@@ -167,6 +175,12 @@ PyObject *results(PyObject *failed, const Tensor *const (&tensors)[N]) {
   return tuple;
 }
 
+// Tells autograd that a tensor of the caller's has changed: one that was saved for a
+// backward pass is then found to have.
+void written(const Tensor *t) {
+  if (t && !t->is_inference()) t->unsafeGetTensorImpl()->bump_version();
+}
+
 // x, w, x_scale, w_scale, bias, residual, act, out, out_dtype, preact, save_preact, products
 PyObject *linear(PyObject *const *a) {
   const Tensor &x = tensor(a[0], "x"), &w = tensor(a[1], "w");
@@ -228,6 +242,7 @@ PyObject *linear(PyObject *const *a) {
   p.w_col = ws.col;
   p.out = given_out->data_ptr();
   if (given_preact) p.preact = given_preact->data_ptr();
+  for (const Tensor *t : {given_out, given_preact}) written(t);
   return results(status(entries.linear, p, index), {given_out, given_preact});
 }
 
@@ -235,6 +250,10 @@ PyObject *linear(PyObject *const *a) {
 PyObject *linear_backward(PyObject *const *a) {
   const Tensor &dout = tensor(a[0], "dout"), &x = tensor(a[1], "x"), &w = tensor(a[2], "w");
   const Tensor *preact = optional_tensor(a[3], "preact");
+  const bool need_dx = truth(a[8]), need_dw = truth(a[9]), need_dbias = truth(a[10]);
+  const Tensor *dx = need_dx ? optional_tensor(a[5], "dx") : nullptr;
+  const Tensor *dw = need_dw ? optional_tensor(a[6], "dw") : nullptr;
+  const Tensor *dbias = need_dbias ? optional_tensor(a[7], "dbias") : nullptr;
   need_2d(x, "x");
   need_2d(w, "w");
   const c10::DeviceIndex index = x.get_device();
@@ -249,10 +268,6 @@ PyObject *linear_backward(PyObject *const *a) {
   if (w.size(0) != p.K)
     raise(PyExc_ValueError, "shape mismatch: x (%lld, %lld), w (%lld, %lld)", ll(p.M), ll(p.K), ll(w.size(0)), ll(p.N));
   p.act = static_cast<int32_t>(integer(a[4]));
-  const bool need_dx = truth(a[8]), need_dw = truth(a[9]), need_dbias = truth(a[10]);
-  const Tensor *dx = need_dx ? optional_tensor(a[5], "dx") : nullptr;
-  const Tensor *dw = need_dw ? optional_tensor(a[6], "dw") : nullptr;
-  const Tensor *dbias = need_dbias ? optional_tensor(a[7], "dbias") : nullptr;
   p.accumulate = truth(a[12]);
   p.products = static_cast<int32_t>(integer(a[13]));
   if (p.act != PHOBOS_ACT_NONE && !preact) raise(PyExc_ValueError, "the gradient of an activation needs preact");
@@ -303,6 +318,7 @@ PyObject *linear_backward(PyObject *const *a) {
   p.dw_row = dws.row;
   p.dw_col = dws.col;
   if (dbias) p.dbias = dbias->data_ptr();
+  for (const Tensor *t : {dx, dw, dbias}) written(t);
   return results(status(entries.linear_backward, p, index), {dx, dw, dbias});
 }
 
@@ -356,6 +372,7 @@ PyObject *rmsnorm(PyObject *const *a) {
   p.out = out->data_ptr();
   if (sum) p.sum = sum->data_ptr();
   if (scale) p.scale = static_cast<float *>(scale->data_ptr());
+  for (const Tensor *t : {out, scale, sum}) written(t);
   return results(status(entries.rmsnorm, p, index), {out, scale, sum});
 }
 
@@ -399,6 +416,7 @@ PyObject *rmsnorm_backward(PyObject *const *a) {
   }
   p.dx = dx->data_ptr();
   if (dweight) p.dweight = dweight->data_ptr();
+  for (const Tensor *t : {dx, dweight}) written(t);
   return results(status(entries.rmsnorm_backward, p, index), {dx, dweight});
 }
 

@@ -18,6 +18,10 @@ pass ``weight.t()`` for a weight stored N x K); the others have unit column stri
 Work is enqueued on ``stream`` (default: torch's current stream); outputs that the
 caller does not pass are allocated there.  Wrong arguments raise ``TypeError`` or
 ``ValueError``, a non-zero status of the library ``PhobosError``.
+
+Autograd does not record these calls.  With gradients enabled, a tensor that requires grad
+is refused (``ValueError``): call the operators under ``torch.no_grad()``, or pair each with
+its backward pass in a ``torch.autograd.Function``, whose methods run so.
 """
 import contextlib
 

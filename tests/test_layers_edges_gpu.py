@@ -214,3 +214,54 @@ def test_slopes_far_from_zero(act, dtype):
     _, _, db = layers.linear_backward(dout, x, w, z, act, need_dx=False, need_dw=False)
     assert (db[:n] == 1).all() and (db[n:2 * n].abs() <= 2.0 ** -40).all()
     assert db[-1].isnan() if act != "relu" else db[-1] == 0
+
+
+def test_autograd_is_told():
+    # refused while gradients are enabled, taken without; a tensor that was written is seen to be
+    x, w = normal((40, 64), F32, 1), weight(64, 48, F32, 2, "nk").requires_grad_()
+    with pytest.raises(ValueError, match="requires grad"):
+        layers.linear(x, w)
+    with torch.no_grad():
+        want = layers.linear(x, w)
+    assert torch.equal(layers.linear(x, w.detach()), want)
+    buf, s, z = torch.ones(40, 48, device="cuda"), torch.ones(40, device="cuda"), torch.ones(40, 64, device="cuda")
+    leaf = torch.ones(40, 48, device="cuda", requires_grad=True)
+    loss = (leaf * buf).sum()
+    layers.linear(x, w.detach(), out=buf)
+    with pytest.raises(RuntimeError, match="inplace"):
+        loss.backward()
+    for t, call in ((buf, lambda: layers.linear(x, w.detach(), preact=buf, save_preact=True)),
+                    (z, lambda: layers.linear_backward(want, x, w.detach(), dx=z)),
+                    (s[:8], lambda: layers.linear_backward(want[:, :8], x, w.detach()[:, :8], dbias=s[:8])),
+                    (z, lambda: layers.rmsnorm(x, None, x, sum=z)),
+                    (s, lambda: layers.rmsnorm_q8(x, scale=s)),
+                    (z, lambda: layers.rmsnorm_backward(x, x, dx=z))):
+        before = t._version
+        call()
+        assert t._version > before
+    with torch.inference_mode():
+        assert torch.equal(layers.linear(x, w, out=torch.empty_like(want)), want)
+
+
+def test_as_an_autograd_function():
+    class Linear(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, w, b):
+            out, z = layers.linear(x, w.t(), b, act="gelu", save_preact=True)
+            ctx.save_for_backward(x, w, z)
+            return out
+
+        @staticmethod
+        def backward(ctx, dout):
+            x, w, z = ctx.saved_tensors
+            dx, dw, db = layers.linear_backward(dout.contiguous(), x, w.t(), z, "gelu")
+            return dx, dw.t(), db
+
+    x, w, b = normal((40, 64), F32, 1), normal((48, 64), F32, 2), vector(48, F32, 3)
+    dout = normal((40, 48), F32, 4)
+    x, w, b = (t.clone().requires_grad_() for t in (x, w, b))
+    Linear.apply(x, w, b).backward(dout)
+    with torch.no_grad():
+        z = layers.linear(x, w.t(), b)
+        want = layers.linear_backward(dout, x, w.t(), z, "gelu")
+    assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1].t()) and torch.equal(b.grad, want[2])

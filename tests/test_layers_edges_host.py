@@ -1,0 +1,27 @@
+"""Refusals of the layer operators' torch interface that need no GPU."""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+from language_fp32_gemm_gb300 import build as lib_build  # noqa: E402
+from language_fp32_gemm_gb300 import layers  # noqa: E402
+
+
+@pytest.fixture(scope="module", autouse=True)
+def lib():
+    lib_build.build()
+
+
+def test_what_requires_grad_is_refused():
+    x, w = torch.zeros(4, 8), torch.zeros(8, 8)
+    p, b = torch.zeros(8, 8, requires_grad=True), torch.zeros(8, requires_grad=True)
+    calls = (lambda: layers.linear(x, p), lambda: layers.linear(p, w), lambda: layers.linear(x, w, bias=b),
+             lambda: layers.linear(x, p.t()), lambda: layers.linear(x, w, residual=p), lambda: layers.linear(x, w, out=p),
+             lambda: layers.linear_q8(x, b, w, b), lambda: layers.linear_backward(x, x, p),
+             lambda: layers.linear_backward(x, x, w, dw=p), lambda: layers.rmsnorm(p), lambda: layers.rmsnorm(x, b),
+             lambda: layers.rmsnorm_q8(x, b), lambda: layers.rmsnorm_backward(p, x), lambda: layers.rmsnorm_backward(x, x, b))
+    for call in calls:
+        with pytest.raises(ValueError, match="requires grad"):
+            call()
+        with torch.no_grad(), pytest.raises(TypeError, match="CUDA"):  # the next check
+            call()
