@@ -328,6 +328,7 @@ PyObject *rmsnorm(PyObject *const *a) {
   const Tensor *weight = optional_tensor(a[1], "weight"), *residual = optional_tensor(a[2], "residual");
   const Tensor *out = optional_tensor(a[4], "out"), *sum = optional_tensor(a[5], "sum");
   const Tensor *scale = optional_tensor(a[7], "scale");
+  if (sum && !residual) raise(PyExc_ValueError, "sum needs a residual: without one, h is x itself");
   need_2d(x, "x");
   const c10::DeviceIndex index = x.get_device();
   const c10::cuda::OptionalCUDAGuard guard(x.device());
@@ -348,8 +349,6 @@ PyObject *rmsnorm(PyObject *const *a) {
     p.residual_row = row_stride(*residual, "residual", p.rows, p.cols, type, index);
     p.residual = residual->data_ptr();
     if (sum) p.sum_row = row_stride(*sum, "sum", p.rows, p.cols, type, index);
-  } else {
-    sum = nullptr;
   }
   if (out) p.out_row = row_stride(*out, "out", p.rows, p.cols, out_type, index);
   if (q8 && scale) vector(*scale, "scale", p.rows, ScalarType::Float, index);

@@ -142,8 +142,9 @@ def linear_backward(dout, x, w, preact=None, act="none", dx=None, dw=None, dbias
 def rmsnorm(x, weight=None, residual=None, eps=1e-6, out=None, sum=None, stream=None):
     """y = h / sqrt(mean(h^2) + eps) * weight over the rows of h = x + residual.
 
-    Returns y, or (y, h) with a residual; ``out`` and ``sum`` give their memory (``sum`` may
-    be ``residual`` or ``x``).  All tensors have x's dtype; the sum is rounded to it first.
+    Returns y, or (y, h) with a residual; ``out`` and ``sum`` give their memory (``sum``, for
+    calls with a residual, may be ``residual`` or ``x``).  All tensors have x's dtype; the
+    sum is rounded to it first.
     """
     if stream is not None:
         with _on(stream, x, weight, residual, out, sum):

@@ -25,3 +25,11 @@ def test_what_requires_grad_is_refused():
             call()
         with torch.no_grad(), pytest.raises(TypeError, match="CUDA"):  # the next check
             call()
+
+
+def test_a_sum_without_a_residual_is_refused():
+    # nothing would be written to it (and the C entry point refuses it)
+    x = torch.zeros(4, 8)
+    for norm in (layers.rmsnorm, layers.rmsnorm_q8):
+        with pytest.raises(ValueError, match="residual"):
+            norm(x, sum=torch.zeros(4, 8))
