@@ -187,6 +187,8 @@ PyObject *linear(PyObject *const *a) {
   const Tensor *x_scale = optional_tensor(a[2], "x_scale"), *w_scale = optional_tensor(a[3], "w_scale");
   const Tensor *bias = optional_tensor(a[4], "bias"), *residual = optional_tensor(a[5], "residual");
   const Tensor *given_out = optional_tensor(a[7], "out"), *given_preact = optional_tensor(a[9], "preact");
+  if (given_out && dtype_or(a[8], given_out->scalar_type()) != given_out->scalar_type())
+    raise(PyExc_TypeError, "out is a %s tensor, not out_dtype", c10::toString(given_out->scalar_type()));
   need_2d(x, "x");
   need_2d(w, "w");
   const c10::DeviceIndex index = x.get_device();

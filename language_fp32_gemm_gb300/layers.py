@@ -85,11 +85,11 @@ def linear(x, w, bias=None, residual=None, act="none", out=None, preact=None, sa
     """act(x w + bias) + residual.
 
     x: M x K, w: K x N, both float32, float16 or bfloat16.  bias (N), residual, out and
-    preact (M x N) have ``out_dtype`` (default: x's).  act: "none", "relu", "gelu" (exact),
-    "gelu_tanh" or "silu".  With ``save_preact`` returns (out, z) with z = x w + bias, which
-    ``linear_backward`` takes; ``preact`` gives its memory.  ``out`` may be ``residual``.
-    products: "auto" chooses by size between "ffma" (CUDA cores, fp32 products) and "tensor"
-    (see the C header).
+    preact (M x N) have ``out_dtype`` (default: that of ``out``, or x's).  act: "none",
+    "relu", "gelu" (exact), "gelu_tanh" or "silu".  With ``save_preact`` returns (out, z) with
+    z = x w + bias, which ``linear_backward`` takes; ``preact`` gives its memory.  ``out`` may
+    be ``residual``.  products: "auto" chooses by size between "ffma" (CUDA cores, fp32
+    products) and "tensor" (see the C header).
     """
     if stream is not None:
         with _on(stream, x, w, bias, residual, out, preact):

@@ -33,3 +33,15 @@ def test_a_sum_without_a_residual_is_refused():
     for norm in (layers.rmsnorm, layers.rmsnorm_q8):
         with pytest.raises(ValueError, match="residual"):
             norm(x, sum=torch.zeros(4, 8))
+
+
+def test_an_output_of_another_dtype_is_refused():
+    # the call used out's own dtype and said nothing
+    x, w, scale = torch.zeros(4, 8), torch.zeros(8, 8), torch.ones(8)
+    q = torch.zeros(8, 8).to(torch.float8_e4m3fn)
+    for call in (lambda out, dtype: layers.linear(x, w, out=out, out_dtype=dtype),
+                 lambda out, dtype: layers.linear_q8(q, scale, q.t(), scale, out=out, out_dtype=dtype)):
+        with pytest.raises(TypeError, match="out_dtype"):
+            call(torch.zeros(4, 8), torch.bfloat16)
+        with pytest.raises(TypeError, match="CUDA"):  # the next check
+            call(torch.zeros(4, 8), torch.float32)
