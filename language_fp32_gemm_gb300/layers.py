@@ -62,16 +62,23 @@ def _named(table, name, what):
 
 @contextlib.contextmanager
 def _on(stream, *tensors):
-    """Allocate and enqueue on another stream than the current one."""
+    """Allocate and enqueue on another stream than the current one, of the tensors' device."""
     import torch
+    first = tensors[0]
+    if not isinstance(first, torch.Tensor) or not first.is_cuda:
+        raise TypeError("operands must be CUDA tensors")
     if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), tensors[0].device)
-    with torch.cuda.stream(stream):
-        yield
-    # the caching allocator must not hand these out again before the stream is past them
-    for t in tensors:
-        if t is not None and t.is_cuda:
-            t.record_stream(stream)
+        stream = torch.cuda.ExternalStream(int(getattr(stream, "cuda_stream", stream)), first.device)
+    elif stream.device != first.device:
+        raise ValueError("the stream is on %s, the tensors on %s" % (stream.device, first.device))
+    try:
+        with torch.cuda.stream(stream):
+            yield
+    finally:
+        # the caching allocator must not hand these out again before the stream is past them
+        for t in tensors:
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(stream)
 
 
 def _done(result, entry):

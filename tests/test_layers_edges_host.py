@@ -45,3 +45,27 @@ def test_an_output_of_another_dtype_is_refused():
             call(torch.zeros(4, 8), torch.bfloat16)
         with pytest.raises(TypeError, match="CUDA"):  # the next check
             call(torch.zeros(4, 8), torch.float32)
+
+
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    # the call went to the current stream of the tensors' device instead
+    from types import SimpleNamespace
+
+    class Stream:
+        device = torch.device("cuda:1")
+
+    class OnDevice0(torch.Tensor):
+        is_cuda = True
+        device = torch.device("cuda:0")
+
+    monkeypatch.setattr(torch.cuda, "Stream", Stream)
+    x = torch.zeros(4, 8).as_subclass(OnDevice0)
+    for call in (lambda: layers.linear(x, x, stream=Stream()), lambda: layers.linear_q8(x, x, x, x, stream=Stream()),
+                 lambda: layers.linear_backward(x, x, x, stream=Stream()), lambda: layers.rmsnorm(x, stream=Stream()),
+                 lambda: layers.rmsnorm_q8(x, stream=Stream()), lambda: layers.rmsnorm_backward(x, x, stream=Stream())):
+        with pytest.raises(ValueError, match="cuda:1"):
+            call()
+    for x in (torch.zeros(4, 8), "x"):
+        for stream in (Stream(), 0, SimpleNamespace(cuda_stream=0)):
+            with pytest.raises(TypeError):
+                layers.rmsnorm(x, stream=stream)
