@@ -22,7 +22,8 @@
  *  - Ownership: A, B and C are caller-owned device pointers; the library never
  *    frees or retains them.  A and B are read only.  C must not overlap A or B
  *    (not checked; the result is undefined).  The library owns its workspace
- *    (per device and stream, grown on demand, released by phobos_release).
+ *    (per device and stream, the per-thread default stream of each thread being
+ *    one of its own; grown on demand, released by phobos_release).
  *    Calls in a stream capture use the workspace of the captured stream, which
  *    is then kept, also when it is outgrown, until phobos_release: a graph's
  *    replays are ordered with the stream's other calls by the caller.  The

@@ -15,6 +15,7 @@
 #include <cstring>
 #include <map>
 #include <mutex>
+#include <tuple>
 #include <utility>
 #include <vector>
 
@@ -148,15 +149,33 @@ struct Buffer {
 };
 // Outgrown buffers that captured graphs may still use, per device, until phobos_release.
 std::vector<std::pair<int, Buffer>> g_retired;
+// A device's stream by its handle, which is one value for the per-thread default streams
+// of all threads: those go by the stream's own id.
+struct StreamKey {
+  int device;
+  bool per_thread;
+  unsigned long long stream;
+  bool operator<(const StreamKey &o) const {
+    return std::tie(device, per_thread, stream) < std::tie(o.device, o.per_thread, o.stream);
+  }
+};
+
+phobos_status_t stream_key(int device, cudaStream_t stream, StreamKey *key) {
+  *key = StreamKey{device, stream == cudaStreamPerThread, reinterpret_cast<uintptr_t>(stream)};
+  if (!key->per_thread || cudaStreamGetId(stream, &key->stream) == cudaSuccess) return PHOBOS_OK;
+  cudaGetLastError();
+  return PHOBOS_ERR_CUDA;
+}
+
 // workspace per (device, stream)
-std::map<std::pair<int, uintptr_t>, Buffer> g_workspaces;
+std::map<StreamKey, Buffer> g_workspaces;
 // tile counters per (device, stream): see runtime_counters
-std::map<std::pair<int, uintptr_t>, Buffer> g_counters;
+std::map<StreamKey, Buffer> g_counters;
 // workspaces of the layer operators per (device, stream): see runtime_workspace
 struct LayerWorkspaces {
   Buffer slot[2];
 };
-std::map<std::pair<int, uintptr_t>, LayerWorkspaces> g_layer_workspaces;
+std::map<StreamKey, LayerWorkspaces> g_layer_workspaces;
 // staging buffers of the host-pointer entry point, per device
 struct Staging {
   Buffer a, b, c;
@@ -286,19 +305,21 @@ phobos_status_t release_stream_workspace(cudaStream_t stream) {
   std::lock_guard<std::mutex> lock(g_mutex);
   int device = 0;
   if (cudaGetDevice(&device) != cudaSuccess) return PHOBOS_ERR_CUDA;
-  phobos_status_t st = PHOBOS_OK;
-  auto counters = g_counters.find({device, reinterpret_cast<uintptr_t>(stream)});
+  StreamKey key;
+  phobos_status_t st = stream_key(device, stream, &key);
+  if (st != PHOBOS_OK) return st;
+  auto counters = g_counters.find(key);
   if (counters != g_counters.end()) {
     if (retire(counters->second, stream) != PHOBOS_OK) st = PHOBOS_ERR_CUDA;
     g_counters.erase(counters);
   }
-  auto layers = g_layer_workspaces.find({device, reinterpret_cast<uintptr_t>(stream)});
+  auto layers = g_layer_workspaces.find(key);
   if (layers != g_layer_workspaces.end()) {
     for (Buffer &b : layers->second.slot)
       if (retire(b, stream) != PHOBOS_OK) st = PHOBOS_ERR_CUDA;
     g_layer_workspaces.erase(layers);
   }
-  auto it = g_workspaces.find({device, reinterpret_cast<uintptr_t>(stream)});
+  auto it = g_workspaces.find(key);
   if (it == g_workspaces.end()) return st;
   if (retire(it->second, stream) != PHOBOS_OK) st = PHOBOS_ERR_CUDA;
   g_workspaces.erase(it);
@@ -644,10 +665,12 @@ phobos_status_t run_tc(int64_t M, int64_t N, int64_t K, float alpha, const float
   const size_t flag_bytes =
       static_cast<size_t>(round_up((tail_flags + split_flags + split_counters) * 4, 256));
   const size_t need = ops_bytes + part_bytes + flag_bytes;
-  Buffer &ws = g_workspaces[{device, reinterpret_cast<uintptr_t>(stream)}];
-  void *const old_ws = ws.ptr;
-  phobos_status_t st = ensure_buffer(ws, need, stream);
+  StreamKey key;
+  phobos_status_t st = stream_key(device, stream, &key);
   if (st != PHOBOS_OK) return st;
+  Buffer &ws = g_workspaces[key];
+  void *const old_ws = ws.ptr;
+  if ((st = ensure_buffer(ws, need, stream)) != PHOBOS_OK) return st;
   if (ws.ptr != old_ws) reuse_b = false;
   float *partials = reinterpret_cast<float *>(static_cast<char *>(ws.ptr) + ops_bytes);
   unsigned *flags =
@@ -840,7 +863,7 @@ phobos_status_t read_status_word(DeviceState &dev, cudaStream_t stream) {
     int device = 0;
     if (cudaGetDevice(&device) != cudaSuccess || cudaDeviceSynchronize() != cudaSuccess) return PHOBOS_ERR_CUDA;
     for (auto &kv : g_counters)
-      if (kv.first.first == device && kv.second.ptr &&
+      if (kv.first.device == device && kv.second.ptr &&
           cudaMemset(kv.second.ptr, 0, kTileCounters * sizeof(unsigned)) != cudaSuccess)
         return PHOBOS_ERR_CUDA;
     return PHOBOS_ERR_TIMEOUT;
@@ -903,15 +926,21 @@ phobos_status_t runtime_state(Runtime *out) {
 
 phobos_status_t runtime_workspace(const Runtime &rt, cudaStream_t stream, int slot, size_t bytes,
                                   void **out) {
-  Buffer &ws = g_layer_workspaces[{rt.device, reinterpret_cast<uintptr_t>(stream)}].slot[slot];
-  const phobos_status_t st = ensure_buffer(ws, bytes, stream);
+  StreamKey key;
+  phobos_status_t st = stream_key(rt.device, stream, &key);
+  if (st != PHOBOS_OK) return st;
+  Buffer &ws = g_layer_workspaces[key].slot[slot];
+  st = ensure_buffer(ws, bytes, stream);
   *out = ws.ptr;
   return st;
 }
 
 phobos_status_t runtime_counters(const Runtime &rt, cudaStream_t stream, unsigned **out) {
-  Buffer &words = g_counters[{rt.device, reinterpret_cast<uintptr_t>(stream)}];
-  const phobos_status_t st = ensure_buffer(words, kTileCounters * sizeof(unsigned), stream, true);
+  StreamKey key;
+  phobos_status_t st = stream_key(rt.device, stream, &key);
+  if (st != PHOBOS_OK) return st;
+  Buffer &words = g_counters[key];
+  st = ensure_buffer(words, kTileCounters * sizeof(unsigned), stream, true);
   *out = static_cast<unsigned *>(words.ptr);
   return st;
 }
@@ -1186,12 +1215,12 @@ phobos_status_t phobos_release(void) {
   };
   for (auto &kv : g_retired) free_on(kv.first, kv.second);
   g_retired.clear();
-  for (auto &kv : g_workspaces) free_on(kv.first.first, kv.second);
+  for (auto &kv : g_workspaces) free_on(kv.first.device, kv.second);
   g_workspaces.clear();
   for (auto &kv : g_layer_workspaces)
-    for (Buffer &b : kv.second.slot) free_on(kv.first.first, b);
+    for (Buffer &b : kv.second.slot) free_on(kv.first.device, b);
   g_layer_workspaces.clear();
-  for (auto &kv : g_counters) free_on(kv.first.first, kv.second);
+  for (auto &kv : g_counters) free_on(kv.first.device, kv.second);
   g_counters.clear();
   for (auto &kv : g_staging) {
     free_on(kv.first, kv.second.a);

@@ -265,3 +265,47 @@ def test_as_an_autograd_function():
         z = layers.linear(x, w.t(), b)
         want = layers.linear_backward(dout, x, w.t(), z, "gelu")
     assert torch.equal(x.grad, want[0]) and torch.equal(w.grad, want[1].t()) and torch.equal(b.grad, want[2])
+
+
+def test_per_thread_default_streams_have_their_own_workspaces():
+    # one handle, a stream a thread: operands split into the workspace and pieces' sums of two
+    # threads at a time, in products and in the GEMM.  Exact sums.
+    import ctypes
+    import threading
+
+    from test_layers_host import structures
+    per_thread = 2  # the handle of the per-thread default stream
+    kind = type("args", (ctypes.Structure,), {"_fields_": structures()["phobos_linear_args_t"]})
+    linear = phobos.library().phobos_linear
+    shapes = [(300, 600, 1024), (40, 520, 4096), (260, 1300, 512), (130, 264, 2080)]
+    work = []
+    for i, (M, N, K) in enumerate(shapes):
+        x, w = small_integers(M, K, F32, 2 * i), small_integers(K, N, F32, 2 * i + 1)
+        work.append((x, w, torch.empty(M, N, device="cuda"), torch.empty(M, N, device="cuda"), x @ w))
+    torch.cuda.synchronize()
+    wrong, ready = [], threading.Barrier(len(shapes))
+
+    def thread(x, w, out, c, want):
+        try:
+            (M, K), N = x.shape, w.shape[1]
+            args = kind(M=M, N=N, K=K, products=2, x=x.data_ptr(), x_row=K, x_col=1, w=w.data_ptr(), w_row=N, w_col=1,
+                        out=out.data_ptr(), out_row=N)
+            ready.wait()
+            for _ in range(20):
+                for _ in range(10):
+                    st = linear(ctypes.c_char_p(bytes(args)), ctypes.c_void_p(per_thread))
+                    st = st or phobos.phobos_sgemm_ex(M, N, K, 1.0, x.data_ptr(), K, w.data_ptr(), N, 0.0, c.data_ptr(), N,
+                                                      per_thread, phobos.PHOBOS_MATH_3XTF32)
+                st = st or phobos.phobos_check_device(per_thread)  # waits for this thread's stream
+                if st or not torch.equal(out.cpu(), want.cpu()) or not torch.equal(c.cpu(), want.cpu()):
+                    wrong.append((tuple(x.shape), st))
+        except BaseException as e:  # noqa: B902
+            wrong.append(e)
+
+    threads = [threading.Thread(target=thread, args=w) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not wrong
+    assert phobos.phobos_release() == phobos.PHOBOS_OK
