@@ -79,13 +79,6 @@ __device__ __forceinline__ void load4(int type, const void *base, int64_t i, int
   else load4<PHOBOS_TYPE_F16>(base, i, n, vec, v);
 }
 
-__device__ __forceinline__ void store4(int type, void *base, int64_t i, int n, bool vec,
-                                       const float (&v)[4]) {
-  if (type == PHOBOS_TYPE_F32) store4<PHOBOS_TYPE_F32>(base, i, n, vec, v);
-  else if (type == PHOBOS_TYPE_BF16) store4<PHOBOS_TYPE_BF16>(base, i, n, vec, v);
-  else store4<PHOBOS_TYPE_F16>(base, i, n, vec, v);
-}
-
 // V consecutive elements as they are stored.  load and store: the first n exist (zeros
 // elsewhere), and with V > 1 the address is aligned for all of them at once;
 // load_any and store_any: any alignment.  16-bit types are converted in pairs.

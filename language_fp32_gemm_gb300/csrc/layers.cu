@@ -190,8 +190,9 @@ phobos_status_t prepare_operands(const LinearArgs &l, const Prepared &pa, const 
                                  const Runtime &rt, cudaStream_t stream) {
   const PrepArgs a = prep_args(l.a, l.M, l.K, l.type, pa, ws), b = prep_args(l.b, l.N, l.K, l.type, pb, ws);
   if (l.type == PHOBOS_TYPE_F32) {
-    if (l.a.kmajor != l.b.kmajor) runtime_launched(cudaSuccess);  // two launches
-    return runtime_launched(launch_split(a, b, rt.sm_count, stream));
+    if (l.a.kmajor == l.b.kmajor) return runtime_launched(launch_split(a, &b, rt.sm_count, stream));
+    const phobos_status_t first = runtime_launched(launch_split(a, nullptr, rt.sm_count, stream));
+    return first == PHOBOS_OK ? runtime_launched(launch_split(b, nullptr, rt.sm_count, stream)) : first;
   }
   phobos_status_t st = PHOBOS_OK;
   if (pa.needed) st = runtime_launched(launch_copy(a, rt.sm_count, stream));

@@ -112,7 +112,8 @@ struct PrepArgs {
   int *exp;       // split only: [rows]
 };
 cudaError_t launch_copy(const PrepArgs &a, int sm_count, cudaStream_t stream);
-cudaError_t launch_split(const PrepArgs &first, const PrepArgs &second, int sm_count, cudaStream_t stream);
+// One launch: both operands (`second` may be null) lie along the contraction, or neither.
+cudaError_t launch_split(const PrepArgs &first, const PrepArgs *second, int sm_count, cudaStream_t stream);
 
 // dz = dout * act'(z), and sums of dz over strips of rows.
 struct DzArgs {

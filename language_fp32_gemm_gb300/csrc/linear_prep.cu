@@ -194,10 +194,7 @@ cudaError_t launch_copy(const PrepArgs &a, int sm_count, cudaStream_t stream) {
                        a.in.ld, static_cast<uint16_t *>(a.hi), a.ld, rows, cols);
 }
 
-namespace {
-
-// One or two operands (`second` may be null) of one kind.
-cudaError_t launch_split_kind(const PrepArgs &first, const PrepArgs *second, int sm_count, cudaStream_t stream) {
+cudaError_t launch_split(const PrepArgs &first, const PrepArgs *second, int sm_count, cudaStream_t stream) {
   const bool strided = !first.in.kmajor;
   // clusters for strided operands: enough CTAs to fill the SMs about twice, at least 64
   // steps each
@@ -217,14 +214,6 @@ cudaError_t launch_split_kind(const PrepArgs &first, const PrepArgs *second, int
   return launch_kernel(strided ? split_kernel<true> : split_kernel<false>, static_cast<unsigned>(ctas),
                        static_cast<unsigned>(all), 256, 0, stream, first, second ? *second : first,
                        static_cast<int>(blocks_first), ctas);
-}
-
-}  // namespace
-
-cudaError_t launch_split(const PrepArgs &first, const PrepArgs &second, int sm_count, cudaStream_t stream) {
-  if (first.in.kmajor == second.in.kmajor) return launch_split_kind(first, &second, sm_count, stream);
-  const cudaError_t e = launch_split_kind(first, nullptr, sm_count, stream);
-  return e == cudaSuccess ? launch_split_kind(second, nullptr, sm_count, stream) : e;
 }
 
 }  // namespace phobos
