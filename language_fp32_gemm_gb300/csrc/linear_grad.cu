@@ -2,6 +2,11 @@
 //   dz = dout * act'(z), rounded to the operands' type, and
 //   dbias_j = sum_i dz_ij of the unrounded values.
 //
+// The tensor cores take dz as 16-bit operands beside 16-bit x and w, so it is rounded once
+// before the two products.  bf16 gradients are then off by 0.0023 of their norm, without
+// that rounding 0.0017 (their own); dz as two 16-bit terms would keep it, for two passes
+// of both products (354 of the 420 us at 4096 x 8192 x 4096) and twice dz's traffic.
+//
 // One pass over dout and z does both: a CTA of 256 threads takes 32 groups of
 // columns (16 bytes of each matrix a group; single elements where rows are not
 // aligned) of a strip of rows, eight rows at a time, sums its columns in registers

@@ -26,12 +26,14 @@
 // order, so that no piece waits for another and the result does not depend on
 // their order.
 //
-// Large products are bound by the MMAs and the power they draw (bf16 8192^3: 638 us,
-// 1.72 PFLOP/s, with bias, GELU, pre-activation and residual 723), short contractions by
-// the epilogue (bf16 8192 x 8192 x 512: 66 and 153 us), few rows by the weight's way in
-// (fp16 16 x 8192 x 8192: 26.6 us, 5.1 TB/s).  8 bits 4096 x 8192 x 8192 with scales,
-// bias, SiLU and residual: 194 us, 2.8 PFLOP/s; fp32 4096^3 with all four:
-// 351 us with its operands' split, 1.2 PFLOP/s of fp16 terms.
+// Large products are bound by the MMAs and the power they draw (bf16 8192^3: 592 to 631
+// us, up to 1.86 PFLOP/s, with tanh GELU, pre-activation and residual 690 to 752; in
+// seconds-long loops at the power cap 712 and, with bias too, 744, at the same clock),
+// short contractions by the epilogue (bf16 8192 x 8192 x 512 over the same buffers: 67 us,
+// with all four 125), few rows by the weight's way in (fp16 16 x 8192 x 8192: 26.6 us,
+// 5.1 TB/s).  8 bits 4096 x 8192 x 8192 with scales, bias, SiLU and residual: 198 us, 2.8
+// PFLOP/s; fp32 4096^3 with tanh GELU, pre-activation and residual: 346 to 355 us with its
+// operands' split, 1.2 PFLOP/s of fp16 terms.
 #pragma once
 
 #include <type_traits>
